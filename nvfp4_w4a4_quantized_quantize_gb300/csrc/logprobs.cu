@@ -534,9 +534,78 @@ __global__ void __launch_bounds__(kMaxThreads, kTop ? 2 : 4) logprob_kernel(cons
 // A stream: p_j from the row's lse, two multiply-adds, one write.  blockIdx.y takes a stretch of the
 // row's vectors.  Where the gradient's rows do not lie on the same 16-byte grid as the logits',
 // elements are written one by one.
+// An lse far from zero is rounded by more than the weights may be off: fp32 holds it to 2^-23 of its
+// size (with the forward's roundings), 2 at 2^24.  From kRounded on, where that is 2^-15, the row's weights
+// are made independent of it: p = exp(z - lse) / sum exp(z - lse), whose differences are exact where
+// they matter.  One block then takes the whole row, as grad may be logits: it has read all of the row
+// before it writes.
 // Measured: 4096 rows of 131072 bf16 logits (1.07 GB read, as much written) in 325 us = 6.6 TB/s, 0.97 of
-// a copy; 2000 rows of 50003 in 62 us = 6.4 TB/s (odd rows begin off the 16-byte grid).
+// a copy; 2000 rows of 50003 in 62 us = 6.4 TB/s (odd rows begin off the 16-byte grid).  With 1000 added to
+// every logit (the row read twice, by one block): 4096 rows 496 us for 338 with cold caches, 64 fp32 rows of
+// 131072 66 for 19.
 constexpr int kGradThreads = 256, kGradUnroll = 4, kGradPerThread = 16;
+constexpr float kRounded = 256.0f;
+
+// z = scale * logit relative to lse.  A masked logit goes far below all others: weight 0, and no 0 * inf.
+__device__ __forceinline__ float grad_relative(float x, float scale, float lse, bool huge)
+{
+    float z = huge ? __fmul_rn(x, scale) - lse : fmaf(x, scale, -lse);
+    asm("max.NaN.f32 %0, %0, %1;" : "+f"(z) : "f"(kClamp));
+    return z;
+}
+
+// log sum exp(scale * logit - lse) of a row, by the whole block: sums relative to the largest term so far, as the
+// terms are off by lse's rounding, up to 2^7 near kHuge.  (Not inlined: its registers would cost the stream a tenth.)
+template <class T>
+__device__ __noinline__ float row_correction(const T* x, int64_t V, float scale, float lse)
+{
+    __shared__ float maxima[kGradThreads / 32], sums[kGradThreads / 32];
+    const Row<T> row(x, 0, 0, V);
+    constexpr int kWidth = Vec<T>::kWidth;
+    constexpr float kLog2e = 1.4426950408889634f;
+    float m = -CUDART_INF_F, s = 0.0f;
+    auto take = [&](const Vec<T>& v) {
+        const float top = grad_relative(v.largest(), scale, lse, false);
+        if (top > m) {
+            s *= pow2((m - top) * kLog2e);
+            m = top;
+        }
+        float part = 0.0f;
+#pragma unroll
+        for (int e = 0; e < kWidth; ++e) part += pow2((grad_relative(v.at(e), scale, lse, false) - m) * kLog2e);
+        s += part;
+    };
+    const int all = row.vectors();
+    int i = threadIdx.x;
+    if (i < row.lo && i < all) {
+        take(row.load(i));
+        i += kGradThreads;
+    }
+    for (; i + (kGradUnroll - 1) * kGradThreads < row.hi; i += kGradUnroll * kGradThreads) {
+        Vec<T> v[kGradUnroll];
+#pragma unroll
+        for (int k = 0; k < kGradUnroll; ++k) v[k] = row.load_whole(i + k * kGradThreads);
+#pragma unroll
+        for (int k = 0; k < kGradUnroll; ++k) take(v[k]);
+    }
+    for (; i < all; i += kGradThreads) take(row.load(i));
+    auto join = [](float& m, float& s, float om, float os) {  // of parts without vectors m is -inf, s 0
+        const float top = fmaxf(m, om);
+        s = (m == top ? s : s * pow2((m - top) * kLog2e)) + (om == top ? os : os * pow2((om - top) * kLog2e));
+        m = top;
+    };
+#pragma unroll
+    for (int d = 16; d; d >>= 1) join(m, s, __shfl_xor_sync(~0u, m, d), __shfl_xor_sync(~0u, s, d));
+    if (threadIdx.x % 32 == 0) {
+        maxima[threadIdx.x / 32] = m;
+        sums[threadIdx.x / 32] = s;
+    }
+    __syncthreads();
+    m = maxima[0];
+    s = sums[0];
+    for (int w = 1; w < kGradThreads / 32; ++w) join(m, s, maxima[w], sums[w]);
+    return m + logf(s);
+}
 
 template <class T>
 __global__ void __launch_bounds__(kGradThreads) logprob_grad_kernel(const __grid_constant__ LogprobGradArgs a)
@@ -557,15 +626,21 @@ __global__ void __launch_bounds__(kGradThreads) logprob_grad_kernel(const __grid
     // From kHuge on the lse is the largest logit itself: the weights are even over the logits equal
     // to it, and the entropy is the logarithm of their number.
     const bool huge = fabsf(lse) >= kHuge;
-    // weights are formed times 2^24, the slope times 2^-24: exp2 flushes what is below 2^-126
-    const float bias = huge ? h : 0.0f, bias2 = 24.0f - bias * 1.4426950408889634f;
-    const float c1 = -gh * a.scale * 5.9604644775390625e-8f, c0 = -(glp + gh * (h - bias)) * a.scale * 5.9604644775390625e-8f;
+    float bias = huge ? h : 0.0f;
     // the row's vectors in even stretches
-    const int all = row.vectors(), first = (int)((int64_t)all * blockIdx.y / gridDim.y), last = (int)((int64_t)all * (blockIdx.y + 1) / gridDim.y);
+    const int all = row.vectors();
+    int first = (int)((int64_t)all * blockIdx.y / gridDim.y), last = (int)((int64_t)all * (blockIdx.y + 1) / gridDim.y);
+    if (!skip && !huge && fabsf(lse) >= kRounded) {
+        if (blockIdx.y) return;
+        first = 0;
+        last = all;
+        bias = row_correction(row.x, a.V, a.scale, lse);
+    }
+    // weights are formed times 2^24, the slope times 2^-24: exp2 flushes what is below 2^-126
+    const float bias2 = 24.0f - bias * 1.4426950408889634f;
+    const float c1 = -gh * a.scale * 5.9604644775390625e-8f, c0 = -(glp + gh * (h - bias)) * a.scale * 5.9604644775390625e-8f;
     auto slope = [&](float x) {
-        float z = huge ? __fmul_rn(x, a.scale) - lse : fmaf(x, a.scale, -lse);
-        asm("max.NaN.f32 %0, %0, %1;" : "+f"(z) : "f"(kClamp));  // a masked logit: weight 0, and no 0 * inf
-        const float p = pow2(fmaf(z, 1.4426950408889634f, bias2));
+        const float z = grad_relative(x, a.scale, lse, huge), p = pow2(fmaf(z, 1.4426950408889634f, bias2));
         return p * fmaf(c1, z, c0);
     };
     const int64_t tv = a.targets && !skip ? (target + row.head) / kWidth : -1;  // the target's vector
