@@ -565,7 +565,8 @@ nvq_status nvfp4_kv_append(const nvq_kv_cache* cache, const void* k, int64_t k_s
  *             last dimension contiguous, 16-byte aligned.  lse  NULL, or fp32 [rows][heads]
  *             contiguous: log of the sum of exponentials (natural).  Rows outside every request
  *             are not written.
- *   B, max_q  requests (<= 2^20); an upper bound of the queries of one request.
+ *   B, max_q  requests (<= 2^20); an upper bound of the queries of one request (<= 65535).  heads * max_q <=
+ *             2^30, and B * kv_heads * (max_q * G / 8 + 1) * (max_blocks * page_size / 8 + 64) < 2^53.
  *   kv_len    int32 [B], new tokens included (they must be in the cache).   block_table as in
  *             nvfp4_kv_plan; entries beyond a request's keys are not read.
  *   workspace, workspace_bytes   at least nvfp4_kv_attention_workspace_size(), 16-byte aligned,

@@ -53,6 +53,7 @@ constexpr float kSlack = 2.0f;       // how far (log2) a score may pass the runn
 constexpr float kLevel = 268435456.0f;      // 2^28: a pass for smaller weights covers as much
 constexpr float kNormalLog2 = -14.0f, kNormal = 6.103515625e-5f;  // the least f16 with all its bits
 constexpr int kBeginKeys = 384;      // keys that a segment's beginning and end cost as much as
+constexpr double kMaxUnits = 9007199254740992.0;  // 2^53 units of work: times the blocks they stay within 64 bits
 
 struct AttnArgs {
     nvq_kv_cache c;
@@ -258,14 +259,11 @@ __global__ void __launch_bounds__(kWarps * 32, kMinCtas) attention_kernel(const 
     for (int b = rb0; b < rb1; ++b) {
         const Request r = request<kRows, T::kStep>(a, b, bad);
         mine += (int64_t)r.units() * r.segs;
-        my_tiles += r.segs;
+        my_tiles += min(r.segs, 1 << 10);  // of so many no one asks how many more
     }
+    my_tiles = min(my_tiles, 1u << 20);
     const int64_t before = block_scan<kThreads>(mine, my_tiles, total, tiles, part, part2);
     if (bad && blockIdx.x == 0) report_status(a.status, NVQ_ERR_ARG, kWhereAttention);
-    if (total >= (1ll << 31)) {
-        if (blockIdx.x == 0 && threadIdx.x == 0) report_status(a.status, NVQ_ERR_ARG, kWhereAttention);
-        return;
-    }
     if (total == 0) return;  // no queries
     // A step for every warp: fewer, fuller blocks have fewer pieces to join.  (At least: a run is then
     // longer than a step, so a block within a segment has a piece of it, which the join counts on.)
@@ -278,14 +276,14 @@ __global__ void __launch_bounds__(kWarps * 32, kMinCtas) attention_kernel(const 
     const float spread = fmaxf(1.1f * sqrtf((float)tiles * (float)total * (kRows == 8 ? 1.0f : 0.25f)), 3.0f * T::kBatch * (float)tiles);
     const int64_t blocks = min((int64_t)gridDim.x, max(min(total / kLeast, (int64_t)spread), (int64_t)1));
     if ((int64_t)blockIdx.x >= blocks) return;
-    int pos = (int)(total * blockIdx.x / blocks);
-    const int end = (int)(total * (blockIdx.x + 1) / blocks);
-    if (before <= pos && pos < before + mine) {
+    // units are counted in 64 bits over the batch (below kMaxUnits, which the host sees to), in 32 within a segment
+    const int64_t begin = total * blockIdx.x / blocks, end = total * (blockIdx.x + 1) / blocks;
+    if (before <= begin && begin < before + mine) {
         int64_t base = before;
         for (int b = rb0; b < rb1; ++b) {
             const Request r = request<kRows, T::kStep>(a, b, bad);
             const int64_t s = (int64_t)r.units() * r.segs;
-            if (pos < base + s) {
+            if (begin < base + s) {
                 run_b = b;
                 run_base = base;
                 break;
@@ -294,8 +292,11 @@ __global__ void __launch_bounds__(kWarps * 32, kMinCtas) attention_kernel(const 
         }
     }
     __syncthreads();
-    int b = run_b, base = (int)run_base;
+    int b = run_b;
     Request rq = request<kRows, T::kStep>(a, b, bad);
+    int seg = (int)((begin - run_base) / rq.units());
+    int64_t seg_at = run_base + (int64_t)seg * rq.units();  // the segment's first unit
+    int from = (int)(begin - seg_at);                       // where the run is in it
 
     // the sign of sm_scale goes into the queries, so that the largest product is the largest score; a
     // scale of 0 becomes the least that keeps -inf times it -inf
@@ -306,18 +307,19 @@ __global__ void __launch_bounds__(kWarps * 32, kMinCtas) attention_kernel(const 
     uint32_t fill = 0, turn = 0;  // stage filled next, stage read next
 
     while (true) {
-        // ---- the portion [pos, pend) of one segment
-        while (rq.segs == 0 || pos >= base + rq.units() * rq.segs) {
-            base += rq.units() * rq.segs;
+        // ---- the run's portion, steps [pbeg, pend), of one segment
+        while (seg >= rq.segs) {
             rq = request<kRows, T::kStep>(a, ++b, bad);
+            seg = 0;
         }
         // a step belongs to the run that its first unit falls in
-        const int seg = (pos - base) / rq.units(), first_unit = base + seg * rq.units() + rq.begin, stop = min(end, first_unit + rq.steps * rq.cost);
-        auto step_at = [&](int u) { return u <= first_unit ? 0 : min((u - first_unit + rq.cost - 1) / rq.cost, rq.steps); };
-        const int pbeg = step_at(pos), pend = step_at(stop);
+        auto step_at = [&](int u) { return u <= rq.begin ? 0 : min((u - rq.begin + rq.cost - 1) / rq.cost, rq.steps); };
+        const int pbeg = step_at(from), pend = step_at((int)min(end - seg_at, (int64_t)rq.units()));
         if (pend <= pbeg) {
-            pos = stop;
-            if (pos >= end) break;
+            seg_at += rq.units();
+            if (seg_at >= end) break;
+            ++seg;
+            from = 0;
             continue;
         }
         const int kvh = seg % a.c.kv_heads, row0 = seg / a.c.kv_heads * kRows;
@@ -753,8 +755,8 @@ __global__ void __launch_bounds__(kWarps * 32, kMinCtas) attention_kernel(const 
         }
         if (!(starts && ends)) {
             // the blocks of the segment, by the runs its first and last step fall in
-            auto block_of = [&](int u) { return (int)((((int64_t)u + 1) * blocks - 1) / total); };
-            const int c0 = block_of(first_unit), c1 = block_of(first_unit + (rq.steps - 1) * rq.cost);
+            auto block_of = [&](int64_t u) { return (int)(((u + 1) * blocks - 1) / total); };
+            const int c0 = block_of(seg_at + rq.begin), c1 = block_of(seg_at + rq.begin + (rq.steps - 1) * rq.cost);
             __threadfence();
             __syncthreads();
             if (threadIdx.x == 0) {
@@ -837,8 +839,10 @@ __global__ void __launch_bounds__(kWarps * 32, kMinCtas) attention_kernel(const 
                 }
             }
         }
-        pos = stop;
-        if (pos >= end) break;
+        seg_at += rq.units();
+        if (seg_at >= end) break;
+        ++seg;
+        from = 0;
         __syncthreads();  // the ring is free again
     }
 }
@@ -888,6 +892,11 @@ extern "C" nvq_status nvfp4_kv_attention(const nvq_kv_cache* cache, const void* 
     NVQ_CHECK_ARG(q_off || B <= rows, NVQ_ERR_SHAPE, "nvfp4_kv_attention: more requests than query rows without q_off");
     NVQ_CHECK_ARG(max_blocks >= 1 && ld_table >= max_blocks && (int64_t)max_blocks * cache->page_size < (1ll << 31), NVQ_ERR_SHAPE,
                   "nvfp4_kv_attention: max_blocks < 1, ld_table < max_blocks, or max_blocks * page_size >= 2^31");
+    // a row tile has 8 rows at least if there are as many, a step 32 keys and 4 units at most
+    NVQ_CHECK_ARG((int64_t)max_q * heads <= (1 << 30) &&
+                      (double)B * cache->kv_heads * ((int64_t)max_q * (heads / cache->kv_heads) / 8 + 1) *
+                              ((double)max_blocks * cache->page_size / 8 + 64) < kMaxUnits,
+                  NVQ_ERR_SHAPE, "nvfp4_kv_attention: heads * max_q above 2^30, or B * heads * max_q * max_blocks * page_size beyond the units of work");
     NVQ_CHECK_ARG(q_stride_t >= 0 && q_stride_h >= 0 && out_stride_t >= 0 && out_stride_h >= cache->head_dim, NVQ_ERR_SHAPE,
                   "nvfp4_kv_attention: a negative stride, or heads of out that overlap");
     NVQ_CHECK_ARG(q_stride_t % 8 == 0 && q_stride_h % 8 == 0 && out_stride_t % 8 == 0 && out_stride_h % 8 == 0 && aligned(q, 16) &&
