@@ -56,17 +56,19 @@ class W4A16Experts:
         self.topk = topk
 
     def forward(self, x, topk_ids, topk_w, out, stream=None):
-        """x [T, H] bf16, topk_ids int32 and topk_w fp32 [T, topk] -> out [T, H] bf16."""
-        T, rows = x.shape[0], x.shape[0] * self.topk
-        ids, w = topk_ids.view(-1), topk_w.view(-1)
-        h, y = _bf16(rows, self.I, device=x.device), _bf16(rows, self.H, device=x.device)
-        a, b = self.w13, self.w2
-        L.nvfp4_gemv(x, a.codes, a.sf, a.sf_cols, a.tscale, 2 * self.I, self.H, h, ids=ids, groups=self.E, x_div=self.topk,
-                     epilogue=L.NVQ_EPI_SWIGLU, stream=stream)
-        L.nvfp4_gemv(h, b.codes, b.sf, b.sf_cols, b.tscale, self.H, self.I, y, ids=ids, groups=self.E,
-                     epilogue=L.NVQ_EPI_ROW_SCALE, row_w=w, stream=stream)
-        row_of = torch.arange(rows, dtype=torch.int64, device=x.device)
-        L.moe_combine(y, row_of, T, self.topk, self.H, out, stream=stream)
+        """x [T, H] bf16, topk_ids int32 and topk_w fp32 [T, topk] -> out [T, H] bf16.  What lies between the calls is
+        allocated, filled and released on the stream that they run on."""
+        with torch.cuda.stream(stream):
+            T, rows = x.shape[0], x.shape[0] * self.topk
+            ids, w = topk_ids.view(-1), topk_w.view(-1)
+            h, y = _bf16(rows, self.I, device=x.device), _bf16(rows, self.H, device=x.device)
+            a, b = self.w13, self.w2
+            L.nvfp4_gemv(x, a.codes, a.sf, a.sf_cols, a.tscale, 2 * self.I, self.H, h, ids=ids, groups=self.E, x_div=self.topk,
+                         epilogue=L.NVQ_EPI_SWIGLU)
+            L.nvfp4_gemv(h, b.codes, b.sf, b.sf_cols, b.tscale, self.H, self.I, y, ids=ids, groups=self.E,
+                         epilogue=L.NVQ_EPI_ROW_SCALE, row_w=w)
+            row_of = torch.arange(rows, dtype=torch.int64, device=x.device)
+            L.moe_combine(y, row_of, T, self.topk, self.H, out)
         return out
 
 
