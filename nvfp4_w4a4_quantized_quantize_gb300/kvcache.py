@@ -78,26 +78,21 @@ class KVBatch:
         self.page_size = page_size
         self.block_table = torch.full((requests, -(-max_len // page_size)), -1, **i32)
         self.free_pages = torch.arange(pages - 1, -1, -1, **i32)  # page 0 is handed out first
-        # lengths and the free count swap between two buffers, step by step
-        self._len = [torch.zeros(requests, **i32) for _ in range(2)]
-        self._free = [torch.full((1,), pages, **i32) for _ in range(2)]
-        self._now = 0
+        # the lengths and behind them the free count, and a place for the next step's: the plan's
+        # outputs are not its inputs, and are copied over them, so that a captured plan advances
+        self._held, self._next = (torch.zeros(requests + 1, **i32) for _ in range(2))
+        self._held[requests] = pages
+        self.kv_len, self.free_count = self._held[:requests], self._held[requests:]
+        self._len_out, self._free_out = self._next[:requests], self._next[requests:]
         self.q_off = torch.zeros(requests + 1, **i32)
         self.slots = torch.full((max_new,), -1, dtype=torch.int64, device=device)
         self.positions = torch.full((max_new,), -1, **i32)
         self.workspace = torch.zeros(L.nvfp4_kv_attention_workspace_size(), dtype=torch.uint8, device=device)
 
-    @property
-    def kv_len(self) -> torch.Tensor:
-        return self._len[self._now]
-
-    @property
-    def free_count(self) -> torch.Tensor:
-        return self._free[self._now]
-
     def plan(self, new_tokens: torch.Tensor, stream=None):
-        """new_tokens int32 [requests]: fills q_off, slots and positions and advances the lengths."""
-        old, new = self._now, 1 - self._now
-        L.nvfp4_kv_plan(new_tokens, self._len[old], self.page_size, self.block_table, self.free_pages, self._free[old],
-                        self._len[new], self._free[new], self.q_off, self.slots, positions=self.positions, stream=stream)
-        self._now = new
+        """new_tokens int32 [requests]: fills q_off, slots and positions and advances kv_len and free_count, in the
+        tensors that they are, so that each replay of a captured call is a step of its own."""
+        L.nvfp4_kv_plan(new_tokens, self.kv_len, self.page_size, self.block_table, self.free_pages, self.free_count,
+                        self._len_out, self._free_out, self.q_off, self.slots, positions=self.positions, stream=stream)
+        with torch.cuda.stream(stream):
+            self._held.copy_(self._next)
