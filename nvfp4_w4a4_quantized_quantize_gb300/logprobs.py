@@ -3,6 +3,7 @@ the rollout's with the trainer's), as an autograd node over token_logprobs and i
 from __future__ import annotations
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _lib as L
 
@@ -20,6 +21,7 @@ class _TokenLogprobs(torch.autograd.Function):
         return logprob.view(targets.shape), entropy.view(targets.shape)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, g_logprob, g_entropy):
         z, t, lse, entropy = ctx.saved_tensors
         if not ctx.needs_input_grad[0]:
@@ -32,5 +34,5 @@ class _TokenLogprobs(torch.autograd.Function):
 
 def token_logprobs(logits: torch.Tensor, targets: torch.Tensor, temperature: float = 1.0):
     """(logprob, entropy), float32 of targets' shape, of logits [..., V] (bf16 or fp32) at `temperature`; rows with a
-    negative target give 0 and take no gradient.  Differentiable in the logits."""
+    negative target give 0 and take no gradient.  Differentiable in the logits, once: a second derivative raises."""
     return _TokenLogprobs.apply(logits, targets, 1.0 / temperature)
