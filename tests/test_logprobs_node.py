@@ -33,3 +33,19 @@ def test_second_derivatives_of_log_probabilities_are_refused(monkeypatch):
     assert (lp - ls.gather(1, t[:, None]).squeeze(1)).abs().max() < 1e-6
     with pytest.raises(RuntimeError, match="once_differentiable"):
         (lp.sum() + g.square().sum()).backward()
+
+
+def test_a_graph_of_the_gradient_that_is_not_used_changes_nothing(monkeypatch):
+    monkeypatch.setattr(logprobs, "L", _Entries)
+    t = torch.tensor([2, 2, 5])
+    grads = []
+    for create in (False, True):
+        z = torch.linspace(-1, 1, 21).view(7, 3).t().requires_grad_(True)  # rows that are not contiguous
+        lp, h = logprobs.token_logprobs(z, t, temperature=0.5)
+        grads.append(torch.autograd.grad(lp.sum() - h.sum(), z, create_graph=create)[0])
+    assert torch.equal(grads[0], grads[1].detach()) and grads[1].requires_grad and not grads[0].requires_grad
+    w = torch.ones(3, requires_grad=True)  # weights of the loss that take a gradient themselves
+    z = torch.randn(3, 7, requires_grad=True)
+    (g,) = torch.autograd.grad((w * logprobs.token_logprobs(z, t)[0]).sum(), z, create_graph=True)
+    with pytest.raises(RuntimeError, match="second derivative"):
+        g.sum().backward()
