@@ -108,6 +108,8 @@ class RolloutModel:
 
     def step(self, batch: KVBatch, tokens: torch.Tensor, new_tokens: list):
         """tokens int64 [sum of new_tokens], request by request -> fp32 logits [tokens, V]."""
+        if not new_tokens or min(new_tokens) < 0 or not tokens.numel() or sum(new_tokens) != tokens.numel():
+            raise ValueError(f"new_tokens: expected counts that add up to the {tokens.numel()} tokens, one at least, got {new_tokens}")
         batch.plan(torch.tensor(new_tokens, dtype=torch.int32, device=tokens.device))
         x = self.embedding[tokens]
         for layer in self.layers:
@@ -116,6 +118,8 @@ class RolloutModel:
 
     def answer(self, batch: KVBatch, prompts: list, steps: int, top_n: int = 4):
         """Greedy answers: (tokens, their log-probabilities, entropies) as [requests, steps] tensors."""
+        if not all(p.numel() for p in prompts):
+            raise ValueError("prompts: a request needs a token at least to continue from, its prompt is empty")
         dev, B = self.embedding.device, len(prompts)
         tokens, new = torch.cat(prompts), [p.numel() for p in prompts]
         kept = []
