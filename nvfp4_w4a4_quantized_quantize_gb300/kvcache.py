@@ -92,6 +92,8 @@ class KVBatch:
     def plan(self, new_tokens: torch.Tensor, stream=None):
         """new_tokens int32 [requests]: fills q_off, slots and positions and advances kv_len and free_count, in the
         tensors that they are, so that each replay of a captured call is a step of its own."""
+        if new_tokens.shape != self.kv_len.shape:
+            raise ValueError(f"new_tokens: expected a count for each of {self.kv_len.numel()} requests, got {tuple(new_tokens.shape)}")
         L.nvfp4_kv_plan(new_tokens, self.kv_len, self.page_size, self.block_table, self.free_pages, self.free_count,
                         self._len_out, self._free_out, self.q_off, self.slots, positions=self.positions, stream=stream)
         with torch.cuda.stream(stream):
