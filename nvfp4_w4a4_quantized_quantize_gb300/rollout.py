@@ -106,14 +106,22 @@ class RolloutModel:
     def __init__(self, embedding: torch.Tensor, layers: list, head: torch.Tensor):
         self.embedding, self.layers, self.head = embedding, layers, W4A16Linear(head)
 
-    def step(self, batch: KVBatch, tokens: torch.Tensor, new_tokens: list):
-        """tokens int64 [sum of new_tokens], request by request -> fp32 logits [tokens, V]."""
-        if not new_tokens or min(new_tokens) < 0 or not tokens.numel() or sum(new_tokens) != tokens.numel():
-            raise ValueError(f"new_tokens: expected counts that add up to the {tokens.numel()} tokens, one at least, got {new_tokens}")
-        batch.plan(torch.tensor(new_tokens, dtype=torch.int32, device=tokens.device))
+    def step(self, batch: KVBatch, tokens: torch.Tensor, new_tokens, max_q: int = None):
+        """tokens int64 [sum of new_tokens], request by request -> fp32 logits [tokens, V].  new_tokens: a count for each
+        request, as a list, or as an int32 tensor on the device with max_q, a bound of the counts (such a step can be
+        captured in a CUDA graph; rows of tokens beyond the counts' sum hold anything)."""
+        if isinstance(new_tokens, torch.Tensor):
+            if max_q is None or not tokens.numel():
+                raise ValueError("new_tokens: counts on the device need max_q, a bound of them, and tokens, one at least")
+        else:
+            if not new_tokens or min(new_tokens) < 0 or not tokens.numel() or sum(new_tokens) != tokens.numel():
+                raise ValueError(f"new_tokens: expected counts that add up to the {tokens.numel()} tokens, one at least, got {new_tokens}")
+            max_q = max(new_tokens)
+            new_tokens = torch.tensor(new_tokens, dtype=torch.int32, device=tokens.device)
+        batch.plan(new_tokens)
         x = self.embedding[tokens]
         for layer in self.layers:
-            x = layer.forward(x, batch, max(new_tokens))
+            x = layer.forward(x, batch, max_q)
         return self.head.forward(_normalized(x), torch.empty(x.shape[0], self.head.N, dtype=torch.float32, device=x.device))
 
     def answer(self, batch: KVBatch, prompts: list, steps: int, top_n: int = 4):

@@ -22,3 +22,8 @@ def test_answers_need_a_prompt():
 def test_steps_need_as_many_tokens_as_they_count(tokens, new):
     with pytest.raises(ValueError, match="new_tokens"):
         _model().step(None, torch.ones(tokens, dtype=torch.int64), new)
+
+
+def test_a_step_with_counts_on_the_device_needs_their_bound():
+    with pytest.raises(ValueError, match="max_q"):
+        _model().step(None, torch.ones(2, dtype=torch.int64), torch.ones(2, dtype=torch.int32))
