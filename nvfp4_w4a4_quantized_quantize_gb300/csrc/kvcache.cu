@@ -322,7 +322,8 @@ extern "C" nvq_status nvfp4_kv_plan(const int32_t* new_tokens, const int32_t* kv
                   "nvfp4_kv_plan: max_blocks < 1, ld_table < max_blocks or free_cap < 1");
     NVQ_CHECK_ARG(room >= 1 && room < (1ll << 31), NVQ_ERR_SHAPE, "nvfp4_kv_plan: room outside [1, 2^31)");
     NVQ_CHECK_ARG(aligned(slots, 8) && aligned(new_tokens, 4) && aligned(kv_len, 4) && aligned(block_table, 4) &&
-                      aligned(free_pages, 4) && aligned(kv_len_out, 4) && aligned(q_off, 4),
+                      aligned(free_pages, 4) && aligned(free_count, 4) && aligned(kv_len_out, 4) && aligned(free_count_out, 4) &&
+                      aligned(q_off, 4) && aligned(positions, 4),
                   NVQ_ERR_ALIGN, "nvfp4_kv_plan: a pointer is not aligned to its elements");
     DeviceStatus* dst = device_status_ptr();
     NVQ_CHECK_ARG(dst, NVQ_ERR_CUDA, "nvfp4_kv_plan: device status word unavailable");
