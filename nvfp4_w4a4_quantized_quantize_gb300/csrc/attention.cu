@@ -722,8 +722,8 @@ __global__ void __launch_bounds__(kWarps * 32, kMinCtas) attention_kernel(const 
             const int gg = i & 7, r = (i >> 3) % kRows, j = (i >> 3) / kRows;
             if (row0 + r >= rows) return;
             const int qi = (row0 + r) / a.group, h = kvh * a.group + (row0 + r) - qi * a.group;
-            const float s = sum == 0.0f ? 0.0f : v_scale / sum;
-            const __nv_bfloat162 pair = __floats2bfloat162_rn(x * s, y * s);
+            const float s = sum == 0.0f ? 0.0f : 1.0f / sum;  // times v_scale last: their product may lie below fp32's range
+            const __nv_bfloat162 pair = __floats2bfloat162_rn(x * s * v_scale, y * s * v_scale);
             *reinterpret_cast<__nv_bfloat162*>(a.out + (int64_t)(rq.first + qi) * a.o_t + (int64_t)h * a.o_h + gg * (kDim / 8) + 2 * j) = pair;
             if (a.lse && gg == 0 && j == 0)
                 a.lse[(int64_t)(rq.first + qi) * a.heads + h] =
