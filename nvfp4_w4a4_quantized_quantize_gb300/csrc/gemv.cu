@@ -452,12 +452,14 @@ __global__ void __launch_bounds__(kGemvMaxWarps * 32, 1) gemv_kernel(const __gri
                     const int r = i >> 5, at = ((r >> 3) * 4 + ((i >> 3) & 3)) * 64 + (i & 7) * 8 + (r & 7);
                     float y = 0.0f;
                     for (int w = 0; w < size; ++w) y += in[w * kPart + at];
-                    y *= x_down[r];
+                    // x's power of two before the weights' scale where it is small, after it where it is large:
+                    // rows near fp32's ends stay within its range on the way
+                    const float down = x_down[r];
+                    y = y * fminf(down, 1.0f) * s_dec * fmaxf(down, 1.0f);
                     if constexpr (kSplit) {
                         store[(nth * kHalves + h) * nx * 32 + i] = y;
                         continue;
                     }
-                    y *= s_dec;
                     if constexpr (kGlu) {
                         if (!h) {
                             gates[team * kPart + at] = silu(y);
@@ -493,10 +495,8 @@ __global__ void __launch_bounds__(kGemvMaxWarps * 32, 1) gemv_kernel(const __gri
                         const int nth = i / (nx * 32), e = i - nth * nx * 32;
                         float y[kHalves] = {};
 #pragma unroll
-                        for (int h = 0; h < kHalves; ++h) {
+                        for (int h = 0; h < kHalves; ++h)
                             for (int q = 0; q < split; ++q) y[h] += gemv_of(base + ((nth * kHalves + h) * nx * 32 + e) * 4, q);
-                            y[h] *= s_dec;
-                        }
                         put(c0 + nth, e, kGlu ? silu(y[0]) * y[kHalves - 1] : y[0]);
                     }
                     gemv_cluster_sync();  // read before they are written again, or before their block ends
