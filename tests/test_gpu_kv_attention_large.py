@@ -111,8 +111,9 @@ def test_bad_query_offsets_leave_the_requests_rows_unwritten(L, work):  # noqa: 
 @pytest.mark.parametrize("amax", [1e-32, 1e30])
 @pytest.mark.parametrize("lens", [[30, 1], [20000, 7]])
 def test_values_of_any_magnitude(L, work, amax, lens):  # noqa: F811
-    """Tensor scales near the ends of fp32's range, even weights over few and many keys."""
+    """Tensor scales near the ends of fp32's range, even weights over few and many keys, positive values (none cancels)."""
     from nvfp4_w4a4_quantized_quantize_gb300.kvcache import tensor_scale
     c = Case(lens, [1, 1], 8, 2, 128, 64, seed=7, q_scale=0.0)
+    c.cache.v_codes &= 0x77
     c.cache.v_tscale.copy_(tensor_scale(amax))
     c.check(L, work)
