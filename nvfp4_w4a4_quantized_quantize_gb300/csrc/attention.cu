@@ -30,10 +30,10 @@
 // whose keys are spread over several blocks is joined by the block that finishes last, always in
 // the order of the keys.
 //
-// Measured (32 query and 4 key heads of 128 values, against a copy's 6.78 TB/s): 64 requests of 65536
-// keys, 2.4 GB, in 442 us = 5.47 TB/s, 0.81; 64 of 1 to 16384 keys, 292 MB, in 68 us = 0.63, of which
-// about 12 us are the beginning and the join; 8 of up to 100k keys of 64 values with 4 new tokens each
-// (16-row tiles, pages of 16), 119 MB, in 58 us; one request of 1000 keys in 8 us.  Instruction issue
+// Measured (this kernel alone, replayed; 32 query and 4 key heads of 128 values, against a copy's 6.78
+// TB/s): 64 requests of 65536 keys, 2.4 GB, in 441 us = 5.48 TB/s, 0.81; 64 of 1 to 16384 keys, 292 MB, in
+// 64 us = 0.67, of which about 12 us are the beginning and the join; 8 of up to 100k keys of 64 values with 4
+// new tokens each (16-row tiles, pages of 16), 119 MB, in 57 us; one request of 1000 keys in 9 us.  Instruction issue
 // bounds it: 605 instructions of a warp per 32 keys of 128 values, 2.2 of 4 issued a cycle, the
 // integer pipe (which expands the codes) 46 % busy, tensor cores 23 %.
 #include <cuda_bf16.h>
