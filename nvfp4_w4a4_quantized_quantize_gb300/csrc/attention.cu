@@ -259,7 +259,7 @@ __global__ void __launch_bounds__(kWarps * 32, kMinCtas) attention_kernel(const 
     for (int b = rb0; b < rb1; ++b) {
         const Request r = request<kRows, T::kStep>(a, b, bad);
         mine += (int64_t)r.units() * r.segs;
-        my_tiles += min(r.segs, 1 << 10);  // of so many no one asks how many more
+        my_tiles += min(r.segs, 1 << 10);  // capped: below they matter only while few, and their sum stays in 32 bits
     }
     my_tiles = min(my_tiles, 1u << 20);
     const int64_t before = block_scan<kThreads>(mine, my_tiles, total, tiles, part, part2);
